@@ -360,10 +360,10 @@ def _append(state):
         b = cache[page].float()
         if turned:
             b = b.transpose(2, 3)
-        # bytes held already move to the block's new scale; what follows the new tokens stays
+        b = torch.where(old[:, None, :, None], b, torch.zeros_like(b))
+        # bytes held already move to the block's new scale; what follows the new tokens is zero
         ee, eo = e[:, :, None, None], e_old[:, :, None, None]
-        b = torch.where(old[:, None, :, None], b * _pow2(eo - ee), b)
-        out = torch.where(new[:, None, :, None], x * _pow2(-ee), b)
+        out = torch.where(new[:, None, :, None], x * _pow2(-ee), b * _pow2(eo - ee))
         if turned:
             out = out.transpose(2, 3)
         cache.view(torch.uint8)[page] = out.to(torch.float8_e4m3fn).view(torch.uint8)
@@ -455,13 +455,13 @@ def _exact_append(s):
                 amax = x.abs().amax(dim=(1, 2))
                 e = torch.ceil(torch.log2(amax.clamp(min=2.0 ** -200) / E4M3_MAX)).clamp_(EXP_MIN, EXP_MAX)
                 body = out[c][page] if c == "k_cache" else out[c][page].transpose(1, 2)
-                body = body.clone()
+                fresh = torch.zeros_like(body)
                 if had:
                     e_old = torch.log2(out[sc][page])
                     e = torch.maximum(e, e_old)
-                    body[:, :had] = _exact_e4m3(body[:, :had] * torch.exp2(e_old - e)[:, None, None])
-                body[:, had:had + hi - lo] = _exact_e4m3(x * torch.exp2(-e)[:, None, None])
-                out[c][page] = body if c == "k_cache" else body.transpose(1, 2)
+                    fresh[:, :had] = _exact_e4m3(body[:, :had] * torch.exp2(e_old - e)[:, None, None])
+                fresh[:, had:had + hi - lo] = _exact_e4m3(x * torch.exp2(-e)[:, None, None])
+                out[c][page] = fresh if c == "k_cache" else fresh.transpose(1, 2)
                 out[sc][page] = torch.exp2(e)
         at += L
     return out
