@@ -457,6 +457,18 @@ int kda_attn_cache_append(const void* k, int64_t ldk, const void* v, int64_t ldv
                           hipStream_t stream);
 
 /*
+ * kda_attn_cache_append_clear -- kda_attn_cache_append, but positions behind the new tokens in the
+ * blocks written into become zero: a block that an earlier sequence has given back keeps nothing
+ * of it, and equal tokens give equal blocks.  Arguments, results and errors are the same otherwise.
+ */
+int kda_attn_cache_append_clear(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype,
+                                const int32_t* cu_seqlens, const int32_t* start_len, int N,
+                                int64_t total_tokens, void* k_cache, void* v_cache, float* k_scale,
+                                float* v_scale, int num_blocks, int block_tokens,
+                                const int32_t* block_table, int max_blocks, int Hk, int dk, int dv,
+                                hipStream_t stream);
+
+/*
  * kda_attn_decode_workspace_size -- bytes of device workspace kda_attn_decode needs: partial
  * outputs where long contexts are cut among workgroups (0 where they are not, and for invalid
  * arguments).

@@ -69,6 +69,8 @@ SIGNATURES = {
                                  _c_p, _c_sz, _c_p]),
     "kda_attn_cache_append": (_c_i, [_c_p, _c_i64, _c_p, _c_i64, _c_i, _c_p, _c_p, _c_i, _c_i64, _c_p, _c_p,
                                      _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p]),
+    "kda_attn_cache_append_clear": (_c_i, [_c_p, _c_i64, _c_p, _c_i64, _c_i, _c_p, _c_p, _c_i, _c_i64, _c_p,
+                                           _c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p]),
     "kda_attn_decode_workspace_size": (_c_sz, [_c_i] * 8),
     "kda_attn_decode": (_c_i, [_c_p, _c_i64, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_i,
                                _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p, _c_p, _c_sz, _c_p]),

@@ -137,13 +137,10 @@ bool decode_sizes(int N, int T, int H, int Hk, int dtype, int block_tokens, int 
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-}  // namespace
-
-KDA_EXPORT int kda_attn_cache_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype,
-                                     const int32_t* cu_seqlens, const int32_t* start_len, int N, int64_t total_tokens,
-                                     void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks,
-                                     int block_tokens, const int32_t* block_table, int max_blocks, int Hk, int dk,
-                                     int dv, hipStream_t stream) {
+int cache_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype, const int32_t* cu_seqlens,
+                 const int32_t* start_len, int N, int64_t total_tokens, void* k_cache, void* v_cache, float* k_scale,
+                 float* v_scale, int num_blocks, int block_tokens, const int32_t* block_table, int max_blocks, int Hk,
+                 int dk, int dv, bool clear, hipStream_t stream) {
     if (!valid_dtype(dtype) || N < 0 || total_tokens < 0 || total_tokens > INT32_MAX) return KDA_ERR_INVALID_ARG;
     if (N == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
     const int st = cache_args(k_cache, v_cache, k_scale, v_scale, num_blocks, block_tokens, block_table, max_blocks,
@@ -158,8 +155,29 @@ KDA_EXPORT int kda_attn_cache_append(const void* k, int64_t ldk, const void* v, 
     if (total_tokens == 0) return KDA_OK;
     kda::AttnAppendArgs a{k, v, ldk, ldv, cu_seqlens, start_len, N, static_cast<int>(total_tokens), Hk,
                           static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale,
-                          num_blocks, block_tokens, block_table, max_blocks};
+                          num_blocks, block_tokens, block_table, max_blocks, clear};
     return to_status(kda::launch_attn_append(a, dtype == KDA_BF16, dk, dv, stream));
+}
+
+}  // namespace
+
+KDA_EXPORT int kda_attn_cache_append(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype,
+                                     const int32_t* cu_seqlens, const int32_t* start_len, int N, int64_t total_tokens,
+                                     void* k_cache, void* v_cache, float* k_scale, float* v_scale, int num_blocks,
+                                     int block_tokens, const int32_t* block_table, int max_blocks, int Hk, int dk,
+                                     int dv, hipStream_t stream) {
+    return cache_append(k, ldk, v, ldv, dtype, cu_seqlens, start_len, N, total_tokens, k_cache, v_cache, k_scale,
+                        v_scale, num_blocks, block_tokens, block_table, max_blocks, Hk, dk, dv, false, stream);
+}
+
+KDA_EXPORT int kda_attn_cache_append_clear(const void* k, int64_t ldk, const void* v, int64_t ldv, int dtype,
+                                           const int32_t* cu_seqlens, const int32_t* start_len, int N,
+                                           int64_t total_tokens, void* k_cache, void* v_cache, float* k_scale,
+                                           float* v_scale, int num_blocks, int block_tokens,
+                                           const int32_t* block_table, int max_blocks, int Hk, int dk, int dv,
+                                           hipStream_t stream) {
+    return cache_append(k, ldk, v, ldv, dtype, cu_seqlens, start_len, N, total_tokens, k_cache, v_cache, k_scale,
+                        v_scale, num_blocks, block_tokens, block_table, max_blocks, Hk, dk, dv, true, stream);
 }
 
 KDA_EXPORT size_t kda_attn_decode_workspace_size(int N, int T, int H, int Hk, int dv, int dtype, int block_tokens,

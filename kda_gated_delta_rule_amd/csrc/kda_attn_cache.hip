@@ -136,10 +136,13 @@ __device__ __forceinline__ void append_page(const AttnAppendArgs& a, const Appen
             } else {
                 *reinterpret_cast<uint2*>(cache + pos * D + 8 * c) = make_uint2(lo, hi);
             }
-        } else if (!TURNED && grown && pos < t0) {
+        } else if (!TURNED && pos < t0) {
+            if (!grown) continue;
             uint2* p = reinterpret_cast<uint2*>(cache + pos * D + 8 * c);
             const uint2 w = *p;
             *p = make_uint2(rescale_e4m3x4(w.x, f_old), rescale_e4m3x4(w.y, f_old));
+        } else if (!TURNED && a.clear) {
+            *reinterpret_cast<uint2*>(cache + pos * D + 8 * c) = make_uint2(0u, 0u);
         }
     }
     if constexpr (TURNED) {
@@ -151,12 +154,14 @@ __device__ __forceinline__ void append_page(const AttnAppendArgs& a, const Appen
             const uint32_t w = *reinterpret_cast<const uint32_t*>(lds + d * (BT + 4) + p);
             if (p >= t0 && p + 4 <= t1) {
                 *out = w;
-            } else if (p < t1 && (p + 4 > t0 || grown)) {
+            } else if (p >= t1) {
+                if (a.clear) *out = 0;
+            } else if (p + 4 > t0 || grown) {
                 const uint32_t old = *out, moved = grown ? rescale_e4m3x4(old, f_old) : old;
                 uint32_t r = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t from = p + j < t0 ? moved : p + j < t1 ? w : old;
+                    const uint32_t from = p + j < t0 ? moved : p + j < t1 ? w : a.clear ? 0u : old;
                     r |= from & (255u << 8 * j);
                 }
                 *out = r;

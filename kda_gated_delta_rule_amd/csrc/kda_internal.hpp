@@ -137,6 +137,7 @@ struct AttnAppendArgs {
     int num_blocks, bt;
     const int32_t* table;  // [N, max_blocks]
     int max_blocks;
+    bool clear;  // positions behind the new tokens become zero
 };
 
 struct AttnDecodeArgs {

@@ -542,7 +542,7 @@ def _attn_cache(k_cache, v_cache, k_scale, v_scale, block_table, N, Hk, dk, dv):
     return nb, bt, block_table.shape[1]
 
 
-def attn_cache_append(k, v, cu_seqlens, start_len, k_cache, v_cache, k_scale, v_scale, block_table):
+def attn_cache_append(k, v, cu_seqlens, start_len, k_cache, v_cache, k_scale, v_scale, block_table, *, clear=False):
     """Quantises new key and value rows into the 8-bit paged cache (kda_attn_cache_append).
 
     k [tokens, Hk, dk], v [tokens, Hk, dv] (bf16 or fp32, token strides as attn_prefill);
@@ -550,7 +550,8 @@ def attn_cache_append(k, v, cu_seqlens, start_len, k_cache, v_cache, k_scale, v_
     already.  k_cache [num_blocks, Hk, block_tokens, dk], v_cache [num_blocks, Hk, dv,
     block_tokens] float8_e4m3fn (block_tokens 16, 32, 64 or 128), k_scale, v_scale [num_blocks, Hk]
     fp32 powers of two, all updated in place; block_table [N, max_blocks] int32 (negative: absent,
-    nothing is written)."""
+    nothing is written).  clear: the positions behind the new tokens in the blocks written into
+    become zero (kda_attn_cache_append_clear) in place of staying as they were."""
     _need(k.dim() == 3 and v.dim() == 3, "k/v [tokens, heads, dim]")
     Tt, Hk, dk = k.shape
     dv = v.shape[-1]
@@ -571,7 +572,8 @@ def attn_cache_append(k, v, cu_seqlens, start_len, k_cache, v_cache, k_scale, v_
         validate_block_table(block_table, nb, spans, bt, distinct=True)
     dev, here = _gpu(k, v, cu_seqlens, start_len, k_cache, v_cache, k_scale, v_scale, block_table)
     with here:
-        st = _lib.load().kda_attn_cache_append(
+        lib = _lib.load()
+        st = (lib.kda_attn_cache_append_clear if clear else lib.kda_attn_cache_append)(
             _ptr(k), ldk, _ptr(v), ldv, _DTYPES[k.dtype], _ptr(cu_seqlens), _ptr(start_len), N, Tt,
             _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb, bt, _ptr(block_table), mb, Hk, dk,
             dv, torch.cuda.current_stream(dev).cuda_stream)
