@@ -228,7 +228,7 @@ def run(state):
         if op == "append":
             kda.attn_cache_append(state["k"], state["v"], state["cu_q"], state["start_len"],
                                   state["k_cache"], state["v_cache"], state["k_scale"],
-                                  state["v_scale"], state["table"])
+                                  state["v_scale"], state["table"], clear=True)
             return _cache(state)
         return {"o": kda.attn_decode(state["q"], state["k_cache"], state["v_cache"],
                                      state["k_scale"], state["v_scale"], state["table"],
