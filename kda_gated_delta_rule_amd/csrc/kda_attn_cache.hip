@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "kda_attn.hpp"
+#include "kda_attn_plan.hpp"
 #include "kda_internal.hpp"
 
 namespace kda {
@@ -252,12 +253,6 @@ __device__ __forceinline__ void split_bf16(const float (&x)[8], bf16x8 (&out)[N]
     }
 }
 
-// Workgroups that a decode call is cut into: two run on each of 256 compute units, so two rounds.
-// With 1536 and 2048, 64 mixed contexts take 193 and 192 us (1024: 199), four long ones 132 and
-// 135 us (1024: 124): the evener rounds cost a start and an end each.
-constexpr int kPieces = 1024;
-constexpr int kStepKeys = 256;  // of a workgroup: 64 for each of its four waves
-
 // How the batch is cut, the same in every workgroup: all sequences into pieces of `steps` steps, a
 // size that makes about a.pieces of them per kv head in all, whatever the lengths.
 struct DecodePlan {
@@ -274,7 +269,7 @@ struct DecodePlan {
         if (a.pieces == 0) return;  // not cut
         int all = 0;
         for (int n = 0; n < a.N; n += kWave) all += wave_total(steps_of(n + lane));
-        steps = max((all + a.pieces - 1) / a.pieces, 1);
+        steps = decode_piece_steps(all, a.pieces, decode_table_steps(a.max_blocks, a.bt));
     }
     __device__ __forceinline__ int pieces_of(int n) const { return (steps_of(n) + steps - 1) / steps; }
     // Sequence and place in it of piece t; sequence -1 past the last.
@@ -629,14 +624,8 @@ int attn_decode_row_groups(int T, int H, int Hk) {
 }
 
 int attn_decode_pieces(int N, int T, int H, int Hk, int bt, int max_blocks) {
-    const int64_t steps = (static_cast<int64_t>(max_blocks) * bt + kStepKeys - 1) / kStepKeys;
     const int64_t per = static_cast<int64_t>(Hk) * attn_decode_row_groups(T, H, Hk);
-    // Short tables go uncut: one launch, no join (1 x 700 positions on 2 kv heads 7.1 us, cut 8.6;
-    // 1 x 2000 on 8: 15.4, cut 9.4; with 32 sequences, a workgroup for each compute unit, 24.9, cut
-    // 29.5; longer ones would make a mixed batch wait for the longest).
-    if (steps <= 4 || (steps <= 8 && N * per >= 256)) return 0;
-    const int64_t pieces = (kPieces + per - 1) / per, most = N * steps;
-    return static_cast<int>(pieces < most ? pieces : most);
+    return decode_pieces(N, per, decode_table_steps(max_blocks, bt));
 }
 
 int64_t attn_decode_most_pieces(int N, int pieces) { return static_cast<int64_t>(pieces) + N; }
