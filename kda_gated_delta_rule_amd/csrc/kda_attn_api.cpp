@@ -2,6 +2,7 @@
 // include/kda.h.  As in kda_api.cpp, every argument check runs here before any HIP call.
 #include "kda.h"
 
+#include <float.h>
 #include <math.h>
 
 #include "kda_check.hpp"
@@ -49,8 +50,9 @@ bool prompt_sizes(int64_t total_q, int64_t total_k, int H, int Hk, int dk, int d
            Hk >= 1 && H % Hk == 0 && supported_dim(dk) && supported_dim(dv) && valid_dtype(dtype);
 }
 
-// |scale| as the kernels take it: a masked score is -inf, which a factor of zero would turn to NaN.
-float nonzero(float scale) { return fmaxf(fabsf(scale), 1e-37f); }
+// |scale| as the kernels take it: a masked score is -inf, which a factor of zero would turn to NaN.  The
+// smallest number above zero stands for it: the largest product q.k there is then scores 2^-20.
+float nonzero(float scale) { return fmaxf(fabsf(scale), FLT_TRUE_MIN); }
 
 }  // namespace
 
