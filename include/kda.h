@@ -347,6 +347,11 @@ int kda_diag_state_stream(float* state_pool, int64_t num_slots, const int32_t* s
  * A query that sees no key gives o = 0, lse = -inf and takes no part in any gradient.  Keys out
  * of a query's sight have no weight whatever their values; a v row that is not finite may make
  * every output of its own sequence NaN.
+ * Range: the weighted sums of v are divided by the sum of the weights at the end, and a weight may
+ * come up to 2^8 times the largest before that (the running maximum moves in steps).  No sum overflows
+ * with |v| (in the cache: 448 times a block's scale) up to 2^119 / Lk; beyond it an output may be inf
+ * or NaN where the exact one is finite.  The products q.k are formed before their factors: the sums
+ * of |q_d k_d| (in the cache: of 448 |q_d|) stay below 2^128.
  * Inputs q, k, v may be rows of a wider array: ldq, ldk, ldv are the strides between tokens in
  * elements (at least heads * dim, multiples of 16 bytes); the heads of a token are contiguous.
  * cu_seqlens entries outside 0 .. total are taken as 0 or total: wrong ones give wrong results,
