@@ -354,8 +354,9 @@ int kda_diag_state_stream(float* state_pool, int64_t num_slots, const int32_t* s
  * of |q_d k_d| (in the cache: of 448 |q_d|) stay below 2^128.
  * Inputs q, k, v may be rows of a wider array: ldq, ldk, ldv are the strides between tokens in
  * elements (at least heads * dim, multiples of 16 bytes); the heads of a token are contiguous.
- * cu_seqlens entries outside 0 .. total are taken as 0 or total: wrong ones give wrong results,
- * but no access outside the arrays.
+ * cu_seqlens is as kda_chunk_prefill's, but its last entry may lie before total: the tokens behind
+ * it belong to no sequence.  Entries outside 0 .. total are taken as 0 or total: wrong ones give
+ * wrong results, but no access outside the arrays.
  */
 
 /*

@@ -58,11 +58,13 @@ def validate_accepted(accepted_len, T):
     _need(all(0 <= x <= T for x in a), "KDA_DEBUG_VALIDATE: accepted_len outside 0..T")
 
 
-def validate_cu_seqlens(cu_seqlens, total_tokens):
+def validate_cu_seqlens(cu_seqlens, total_tokens, padded=False):
+    """Ranges that begin at 0, do not decrease and end at total_tokens, or before it where padded."""
     cu = _host(cu_seqlens)
     _need(len(cu) >= 1 and cu[0] == 0, "KDA_DEBUG_VALIDATE: cu_seqlens[0] != 0")
     _need(all(b >= a for a, b in zip(cu[:-1], cu[1:])), "KDA_DEBUG_VALIDATE: cu_seqlens decreases")
-    _need(cu[-1] == total_tokens, "KDA_DEBUG_VALIDATE: cu_seqlens[-1] != total_tokens")
+    _need(padded or cu[-1] == total_tokens, "KDA_DEBUG_VALIDATE: cu_seqlens[-1] != total_tokens")
+    _need(cu[-1] <= total_tokens, "KDA_DEBUG_VALIDATE: cu_seqlens[-1] past total_tokens")
 
 
 def validate_snapshots(snapshot_slots, slot_idx, num_slots):
@@ -436,8 +438,8 @@ def _attn_prompt(q, k, v, cu_seqlens, cu_seqlens_k):
     _contig(cu_seqlens, cu_seqlens_k)
     lds = _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v")
     if debug_validate_enabled():
-        validate_cu_seqlens(cu_seqlens, Tq)
-        validate_cu_seqlens(cu_seqlens_k, Tk)
+        validate_cu_seqlens(cu_seqlens, Tq, padded=True)
+        validate_cu_seqlens(cu_seqlens_k, Tk, padded=True)
     return (Tq, Tk, cu_seqlens.shape[0] - 1, H, Hk, dk, dv), cu_seqlens_k, lds
 
 
@@ -565,7 +567,7 @@ def attn_cache_append(k, v, cu_seqlens, start_len, k_cache, v_cache, k_scale, v_
     _contig(cu_seqlens, start_len)
     ldk, ldv = _token_stride(k, "k"), _token_stride(v, "v")
     if debug_validate_enabled():
-        validate_cu_seqlens(cu_seqlens, Tt)
+        validate_cu_seqlens(cu_seqlens, Tt, padded=True)
         start, cu = validate_cache_lens(start_len, mb * bt, "start_len"), _host(cu_seqlens)
         spans = [(s, s + b - a) for s, a, b in zip(start, cu[:-1], cu[1:])]
         _need(all(e <= mb * bt for _, e in spans), "KDA_DEBUG_VALIDATE: tokens past max_blocks")
