@@ -361,8 +361,8 @@ int kda_diag_state_stream(float* state_pool, int64_t num_slots, const int32_t* s
 
 /*
  * kda_attn_prefill_workspace_size -- bytes of device workspace kda_attn_prefill needs: partial
- * outputs of the tiles that several workgroups share, where total_k allows for such (at most 136
- * MB; 0 where it does not, and for invalid arguments).
+ * outputs of the tiles that several workgroups share, where total_k allows for such (at most
+ * 68,157,440; 0 where it does not, and for invalid arguments).
  */
 size_t kda_attn_prefill_workspace_size(int num_seqs, int64_t total_q, int64_t total_k, int H, int Hk,
                                        int dk, int dv, int dtype);
@@ -374,7 +374,10 @@ size_t kda_attn_prefill_workspace_size(int num_seqs, int64_t total_q, int64_t to
  *   v             [total_k, Hk, dv] dtype, ldv
  *   cu_seqlens_q, cu_seqlens_k  [num_seqs + 1] int32 on the device, as kda_chunk_prefill's; the
  *                 same array for whole prompts, more keys than queries for a prompt's later
- *                 chunk.  Empty sequences and sequences without keys are allowed.
+ *                 chunk.  Empty sequences and sequences without keys are allowed.  Of up to 64
+ *                 sequences the tiles with most work come first and long ones are shared among
+ *                 workgroups; with more than 64 sequences a tile is one workgroup's, in the
+ *                 sequences' order, so one much longer than the others is waited for.
  *   o             [total_q, H, dv] dtype (output; tokens of no sequence are left as they were)
  *   lse           [total_q, H] fp32 (output), or NULL
  *   workspace     at least kda_attn_prefill_workspace_size(...) bytes (may be NULL for 0);

@@ -291,7 +291,9 @@ struct WorkItem {
 // gone through by work, most first, so that a workgroup that starts late has little to do; tile j
 // (of the queries: from the last, of the keys: from the first) has min(cap, max(A - 4 j, 0)) units,
 // A from the keys, cap from the queries that there are to see them.  More than 64 sequences go in
-// their order, unshared.
+// their order, unshared: of documents of 100 tokens and one of 8192 behind them, 8 heads on 1 of 128 in
+// bf16, gradients take 585 us with 64 sequences and 1770 with 65 (32 heads on 8: 1925 and 1900, which
+// fill the card by themselves; the forward 191 and 191, 597 and 583).
 //
 // With SPLIT, where a tile has more than an even share of the whole among `slots` workgroups (and more
 // than `least` units, below which a part is not worth its sum), every tile of more than `level`

@@ -31,7 +31,7 @@ int prompt_args(const void* q, int64_t ldq, const void* k, int64_t ldk, const vo
     if (!valid_rows(k, total_k, ldk, static_cast<int64_t>(Hk) * dk, dtype)) return KDA_ERR_INVALID_ARG;
     if (!valid_rows(v, total_k, ldv, static_cast<int64_t>(Hk) * dv, dtype)) return KDA_ERR_INVALID_ARG;
     if (!cu_q || !aligned16(cu_q) || !cu_k || !aligned16(cu_k)) return KDA_ERR_INVALID_ARG;
-    // offsets inside a tile of 64 tokens are 32-bit
+    // offsets inside a tile of 128 tokens in bf16, of 64 in fp32, are 32-bit
     if (ldq > (1 << 22) || ldk > (1 << 22) || ldv > (1 << 22) || static_cast<int64_t>(H) * dv > (1 << 22))
         return KDA_ERR_INVALID_ARG;
     // token counts as in cu_seqlens (int32), element offsets within int64

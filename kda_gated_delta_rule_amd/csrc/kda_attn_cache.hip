@@ -76,7 +76,8 @@ __device__ __forceinline__ AppendBlock find_block(const AttnAppendArgs& a, int t
 // A workgroup for each page that the call writes into, kv head, and k or v: it alone knows the page's
 // largest value, and a page's scale and bytes have one writer.  128,076 tokens of 8 heads, 128 + 128,
 // from bf16: 154-170 us, 4.6-5.1 TB/s of the bytes read and written, a large copy's rate (4.9).
-// 64 sequences of one token: 8 us, the chain from the lengths over the table to the page.
+// 64 sequences of one token: 8 us, the chain from the lengths over the table to the page; 12 us where half
+// of the pages raise their scale, whose older numbers go through the registers again.
 //
 // One page and kv head of k (TURNED false) or v (true).  The new rows stay in registers between
 // the search for their largest value and their conversion.
